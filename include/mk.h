@@ -435,9 +435,9 @@ mk_status mk_chunk_attention(mk_state *st, int layer, const mk_chunk *chunk, con
  *                 when every draft was accepted
  *   out_accept_prob  dev float32 [n_streams][T-1] or NULL: min(1, p/q) of each draft
  * The row that the token is drawn from has weights that are multiples of 2^-44
- * of its largest (rounded up to a power of two), each good to 2^-39 of itself
- * and half a multiple, so a token below 2^-45 of the largest has none; sums are
- * exact.  A test is decided by float32 sums (good to 2^-18) where it clears its
+ * of a power of two above its largest (2.1 times it at most), each good to
+ * 2^-36 + 2^-46 |logit / temperature| of itself and half a multiple, so a token
+ * below 2^-45 of that power has none; sums are exact.  A test is decided by float32 sums (good to 2^-18) where it clears its
  * border by 2^-16, else by such weights.  The tokens are those of the formulas
  * in 64 bits wherever these weights can tell, and do not depend on the batch.
  * A draft below 2^-120 of its row's largest is not accepted.  out_accept_prob is

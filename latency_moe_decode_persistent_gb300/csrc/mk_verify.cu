@@ -8,9 +8,9 @@
 // Where a cumulative sum over 10^5 entries crosses a random number is decided
 // by its last digits: with weights good to 2^-23, one draw in some tens falls
 // on the wrong side of a border.  So a weight is an integer multiple of 2^-44
-// of the power of two above the row's largest, good to about 2^-39, and all
-// sums are integers: exact, so independent of how a row is cut and of the
-// other streams.  With
+// of the power of two above the row's largest, good to 2^-36 + 2^-46 |logit /
+// temperature| of itself (below), and all sums are integers: exact, so
+// independent of how a row is cut and of the other streams.  With
 //   y = logit * (log2 e / temperature) = (k + f) / 32 + yl,  k an integer,
 //   |f| <= 1/2 (a two-float product), 2^y = 2^(k div 32) T[k mod 32] e^z
 // T comes from 32 entries that a warp's lanes hold (a shuffle instead of
@@ -19,6 +19,10 @@
 // with fewer instructions, but this GPU's FP64 rate is 1/60 of its FP32 rate,
 // and conversions run at an eighth of it, so floats become integers by adding
 // 3 * 2^k and taking the bits.
+// Error: e^z - 1 = zh + w, w below 2^-14, is rounded to half a step of w and its
+// product with T to three half steps of 2^-13 at most, together below 2^-36 of
+// the weight (2^-36.3 over 400,000 neighbouring logits in an exact emulation); yl,
+// within 1.5 steps of y, has 24 bits, which |y| 2^-46.4 covers.
 //
 // Such a weight costs some 50 instructions, so only the row that the token is
 // drawn from has them.  The other rows are needed for the tests' normalisers
@@ -54,6 +58,11 @@ __device__ __forceinline__ Scale scale_of(float t) {
     s.lo = __fdiv_rn(fmaf(-s.hi, t, 1.44269502162933349609375f) + 1.925963033500975e-8f, t);
     return s;
 }
+// An integer above the unrounded exponent of a logit, and of any below it, from the
+// rounded product y: both roundings, of the product and of hi, leave at most half
+// a step and one of y, and 2^-22 |y| is two at least.  (The integer at or above y
+// itself will not do: a product that is rounded down to it would weigh more than 1.)
+__device__ __forceinline__ float above(float y) { return floorf(fmaf(fabsf(y), 0x1p-22f, y)) + 1.f; }
 __device__ __forceinline__ bool good_t(float t) { return t >= 1e-3f && t <= 1e3f; }
 
 using f2 = unsigned long long;  // two floats side by side
@@ -83,7 +92,7 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b) { return fma2(b, pk(-1.f), a); }
 
 constexpr uint32_t C1 = 0x40400000u, C2 = 0x35400000u;  // bits of 3 and of 3 * 2^-22
 
-// 2^(y - yref) of two logits, yref an integer not below either y, as (h + l) * p2,
+// 2^(y - yref) of two logits, yref an integer above either (`above`), as (h + l) * p2,
 // p2 a power of two; y below yref - range counts as yref - range (range < 126).
 // All 32 lanes call; T: this lane's table entry (2^(lane/32) as two floats).
 struct Pow2 {
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(NT) verify_sums_kernel(VerifyP p) {
     // join_row lets pass
     const bool bad = nan || !good_t(t) || !(y < YMAX);
     if (!bad && y > -YMAX - 64.f) {
-        out.yref = ceilf(y);
+        out.yref = above(y);
         // logits far below (masked ones, the padding) as one that weighs 2^-110: finite,
         // so that the product's rest stays a number
         const float far = (out.yref - 110.f) / c.hi;
@@ -341,7 +350,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) verify_draw_ker
         }
         const bool fin = good_t(t) && fabsf(ld * c.hi) < YMAX;
         const float l = fin ? ld : 0.f;
-        ey = ceilf(l * c.hi);
+        ey = above(l * c.hi);
         const Pow2 e = powers(l, l, c, (int)ey, 120.f, tab);
         float p2, x;
         up(e.h, eh, x);
