@@ -360,7 +360,8 @@ mk_status mk_layer_forward_noalloc(const mk_model_desc *desc, const mk_layer_wei
  * mk_chunk_attention and mk_verify_drafts use the state's workspace, so graphs
  * that hold calls of one state must not run side by side; two states may.
  * Calls with n_rows = 0 do nothing.  After a device error outputs of the call
- * are unspecified (memory that is not an output stays untouched). */
+ * are unspecified, except where mk_verify_drafts says what they are (memory that
+ * is not an output stays untouched). */
 
 /* Append a chunk's keys and values to the cache: rotate-half RoPE of q and k at
  * each row's position (the state's table, products in float32), k and v stored
@@ -442,7 +443,8 @@ mk_status mk_chunk_attention(mk_state *st, int layer, const mk_chunk *chunk, con
  * in 64 bits wherever these weights can tell, and do not depend on the batch.
  * A draft below 2^-120 of its row's largest is not accepted.  out_accept_prob is
  * good to 2^-17.
- * vocab at most 2^18.  Device-side errors, for which the stream gets n = 0 and token -1:
+ * vocab at most 2^18.  Device-side errors, for which the stream gets n = 0 and token -1
+ * (its out_accept_prob is unspecified; the call's other streams get their answers):
  * a row without a finite logit, NaN or +inf among the logits, |logit| /
  * temperature of 9e4 or more at a row's maximum, a draft probability that is
  * negative, NaN or infinite where the call reads it (MK_ERR_RANGE); a token

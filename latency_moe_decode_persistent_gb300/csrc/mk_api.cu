@@ -39,6 +39,7 @@ struct mk_state {
     AttnWs attn_ws{};
     int attn_grid = 0;
     float2 *d_vtab = nullptr;
+    int *d_vgone = nullptr;
     VerifyPart *d_vpart = nullptr;
     cudaStream_t last_stream = nullptr;
     int32_t *trace = nullptr;
@@ -440,6 +441,7 @@ mk_status mk_create(const mk_model_desc *desc, const mk_weights *w, mk_state **o
             return bail(fail(st, MK_ERR_CUDA, "copy of the power table"));
         const size_t n = (size_t)MK_VERIFY_STREAMS * d.max_T * mk_verify_slices(d.vocab);
         if ((r = dalloc(st, &st->d_vpart, n * sizeof(VerifyPart))) != MK_OK) return bail(r);
+        if ((r = dalloc(st, &st->d_vgone, sizeof(int))) != MK_OK) return bail(r);
     }
     *out = st;
     return MK_OK;
@@ -853,6 +855,8 @@ mk_status mk_verify_drafts(mk_state *st, int n_streams, const int32_t *draft_tok
         p.part = st->d_vpart;
         p.tab = st->d_vtab;
         p.ctrl = st->ctrl;
+        p.gone = st->d_vgone;
+        p.first = b == 0;
         p.T = T;
         p.V = d.vocab;
         const int n = (int)(n_streams - b < MK_VERIFY_STREAMS ? n_streams - b : MK_VERIFY_STREAMS);

@@ -193,6 +193,8 @@ struct VerifyP {
     VerifyPart *part;                  // [streams * T][nsl]
     const float2 *tab;                 // [32] 2^(i/32) as two floats
     Ctrl *ctrl;
+    int *gone;                         // an error before the call: written by its first launch, read by all
+    int first;                         // this is that launch
     int T, V, nsl, slice;
     int len;                           // entries of a warp's range in the draw
 };

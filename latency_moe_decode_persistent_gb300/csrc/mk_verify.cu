@@ -194,7 +194,11 @@ __global__ void __launch_bounds__(NT) verify_sums_kernel(VerifyP p) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) x[i] = i * NT + tid < n ? __ldg(src + i * NT + tid) : -CUDART_INF_F;
     const float t = __ldg(p.temps + row / p.T);
-    if (__syncthreads_or(aborted(p.ctrl))) return;
+    // an earlier call's error; what this call raises, in the draws of this launch and
+    // the ones before, keeps no other stream from its answer
+    const bool gone = p.first ? aborted(p.ctrl) : *(volatile const int *)p.gone != 0;
+    if (p.first && sl == 0 && row == 0 && tid == 0) *p.gone = gone;
+    if (__syncthreads_or(gone)) return;
     float m = -CUDART_INF_F;
     bool nan = false;
 #pragma unroll
@@ -360,14 +364,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) verify_draw_ker
         el = fin ? el * p2 : 0.f;
     }
     if (tid == 0) odd = 0;
-    const bool gone = __syncthreads_or(aborted(p.ctrl));  // (the sums raise nothing)
     cl.sync();                                    // every CTA is there to be written to
     cudaGridDependencySynchronize();
     if (wid < T) {
         const Row r = join_row(p, s * T + wid, lane);
         if (lane == 0) rows[wid] = r;
     }
-    __syncthreads();
+    const bool gone = __syncthreads_or(tid == CT - 1 && *(volatile const int *)p.gone);
     if (wid == 0) {
         // lane i tests draft i+1
         const Row tr = rows[lane < T ? lane : 0];
@@ -392,7 +395,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(CT) verify_draw_ker
         if (lane == 0) wrong = anyin ? 2 : anybad ? 1 : 0;
     }
     __syncthreads();
-    const bool dead = gone || wrong;              // (agreed on by the cluster at its first meeting)
+    const bool dead = gone || wrong;              // (the same in all CTAs of the cluster)
     const int b = min(V, (rank * CW + wid) * len), e = min(V, b + len);
     const Cache w{cache + wid * len, reinterpret_cast<uint16_t *>(cache + CW * len) + wid * len};
     int turn = 0;
