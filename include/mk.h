@@ -399,9 +399,11 @@ mk_status mk_kv_read(mk_state *st, int layer, const mk_chunk *chunk, const mk_kv
  *   out  dev [n_rows][n_q_heads][head_dim] softmax(q k / sqrt(head_dim)) v;
  *        must not overlap q
  * Scores, softmax statistics and outputs are held in float32; probabilities
- * are rounded to bf16 (bf16 cache) or f16 (FP8 cache) for the product with v.
- * With an FP8 cache queries become f16 too: one beyond 65504, infinities
- * included, ends in MK_ERR_RANGE, and a NaN stays in its row.  A row uses the
+ * are rounded to bf16 (bf16 cache) or f16 (FP8 cache) for the product with v;
+ * in f16, one below 2^-25 of its row's largest becomes a multiple of at most
+ * 2^-35 of that.  With an FP8 cache queries become f16 too: elements below 2^-17
+ * become multiples of 2^-24, one beyond 65504, infinities included, ends in
+ * MK_ERR_RANGE, and a NaN stays in its row.  A row uses the
  * entries at its own position and before alone, whatever those behind hold
  * (infinities and NaN included; rows before such an entry of their own chunk
  * are computed anew, slowly).  The key axis of a long context is split over the

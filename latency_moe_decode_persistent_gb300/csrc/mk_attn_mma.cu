@@ -21,9 +21,9 @@
 // end.
 //
 // The online softmax keeps a reference maximum per row and moves it, with a
-// rescale of O in TMEM, only when the row's maximum has grown by more than
-// 2^8: probabilities stay below 2^8, which 16-bit floats hold as well as
-// numbers below 1, and the rescale leaves the common path.
+// rescale of O in TMEM, only when the row's maximum has grown by more than 2^8
+// (bf16) or 2^4 (f16, FP8 caches): probabilities may exceed 1 by that much, and
+// the rescale leaves the common path.
 //
 // Behind a stream's last position a page holds whatever was there: 0 * NaN must
 // not reach O.  The last page's box therefore starts `sh` rows early (rows of a
@@ -63,6 +63,14 @@ struct Cfg {
     // are not cut to pieces: their mean over 44 drawn calls is 29.3 us with OV + 1,
     // 29.0 with OV, 29.3 with OV - 1; 137 tokens alone 20.5 with OV + 2, 14.4 with OV.
     static constexpr int OV = FP8 ? 5 : 3, MIN_COST = OV;
+    // A row's reference maximum moves when its maximum has grown by more than GROW powers
+    // of two, and its probabilities, their sum and its output are held times 2^BIAS, which
+    // cancels.  In f16 2^(BIAS + GROW) may be the largest, and numbers below 2^-14 lose
+    // bits: with 2^11 a key counts with all bits down to 2^-25 of its row's largest, and as
+    // a multiple of 2^-35 of it below (without the bias, 65536 keys 18 nats below one whose
+    // V is 0 vanished).  Moves cost time: chunks up to 2048 over FP8 take 190.5 us with a
+    // GROW of 8, 190.6 with 4, 198 with 2, 207 with 1.  A bf16's range needs none of it.
+    static constexpr float GROW = FP8 ? 4.f : 8.f, BIAS = FP8 ? 11.f : 0.f;
     static constexpr int RING = FP8 ? 3 : 5;        // tiles the MMAs read
     static constexpr int RAW = FP8 ? 4 : 0;         // tiles of codes
     static constexpr uint32_t Q = 0, KV = 2 * TILE, RAWS = KV + RING * TILE, BARS = RAWS + RAW * RAW_TILE;
@@ -396,7 +404,7 @@ attn_mma_kernel(const __grid_constant__ MmaP p, const __grid_constant__ CUtensor
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(mx4[k], s[124 + k]);
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                if (__any_sync(0xffffffffu, mine && ((mx - m) * sc > 8.f || (m == -CUDART_INF_F && mx > m)))) {
+                if (__any_sync(0xffffffffu, mine && ((mx - m) * sc > C::GROW || (m == -CUDART_INF_F && mx > m)))) {
                     const float mn = fmaxf(m, mx), al = m == -CUDART_INF_F ? 0.f : ex2((m - mn) * sc);
                     m = mn;
                     l *= al;
@@ -412,7 +420,7 @@ attn_mma_kernel(const __grid_constant__ MmaP p, const __grid_constant__ CUtensor
                         }
                     }
                 }
-                const float mr = m == -CUDART_INF_F ? 0.f : -m * sc;
+                const float mr = m == -CUDART_INF_F ? 0.f : C::BIAS - m * sc;
                 const uint64_t sc2 = f2(sc, sc), mr2 = f2(mr, mr);
                 uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
