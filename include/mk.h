@@ -184,8 +184,9 @@ typedef struct {
  * access outside the caller's tensors follows a bad value): row_offsets ascend
  * from 0 and end at n_rows or before, contexts are >= 0, a stream's positions
  * fit its page-table row, and every page that the call touches lies in
- * [0, n_pages).  Page-table entries that no position of the call needs are not
- * read. */
+ * [0, n_pages).  Offsets or contexts that are bad for any stream, also for one
+ * without rows, leave the whole call without effect.  Page-table entries that no
+ * position of the call needs are not read. */
 typedef struct {
     int n_streams;                   /* >= 1                                          */
     int n_rows;                      /* rows of the packed tensors                    */

@@ -8,8 +8,8 @@
 // (five shuffles; more streams search in memory).
 //
 // Measured (32/4 heads of 128, one GB300; of the copy bandwidth): 37319 rows
-// appended to FP8 caches in 126 us (5.8 TB/s, 85 %), 2047 rows to bf16 ones in 14 us (3.0
-// TB/s; the kernel alone 11 us), 6 rows in 6 us; 39106 rows of FP8 entries read
+// appended to FP8 caches in 126 us (5.8 TB/s, 85 %), 2047 rows to bf16 ones in 13 us (3.1
+// TB/s), 6 rows in 6 us; 39106 rows of FP8 entries read
 // back in 29 us (4.2 TB/s; the kernel alone 23 us), 129 rows in 5 us.
 #include "mk_chunk.cuh"
 
@@ -21,16 +21,24 @@ struct RowAt {
     int phys;   // physical page
 };
 
+// stream i's part of the chunk's description, as the attention's plan checks it
+__device__ __forceinline__ bool good_stream(const ChunkP &c, int i, int o0, int o1, int ctx) {
+    return (i > 0 || o0 == 0) && o0 >= 0 && o1 >= o0 && o1 <= c.n_rows && ctx >= 0 && (long long)ctx + (o1 - o0) <= c.max_pos;
+}
+
 // The lanes of a warp look up packed rows r (of their own; behind the rows:
-// none).  Memory safety rests on the checks here alone: nothing is read or
-// written for a row that fails one.
-__device__ RowAt row_at(const ChunkP &c, const KvP &kv, Ctrl *ctrl, long long r) {
+// none).  A description that is bad for any stream leaves no row (`good`: of more
+// than 32 streams, which the block has checked; fewer are checked here).  Memory
+// safety rests on the checks of a row's own stream: nothing is read or written
+// for a row that fails one.
+__device__ RowAt row_at(const ChunkP &c, const KvP &kv, Ctrl *ctrl, long long r, bool good) {
     const int lane = threadIdx.x % 32, S = c.S;
-    const int first = __ldg(c.off), last = __ldg(c.off + S);
-    const bool desc = first == 0 && last >= 0 && last <= c.n_rows;
-    int s = 0, o0 = 0, o1 = 0;  // the last stream that begins at r or before
+    const int last = __ldg(c.off + S);
+    int s = 0, o0 = 0, o1 = 0, ctx = 0;  // the last stream that begins at r or before
     if (S <= 32) {
-        const int o = lane < S ? __ldg(c.off + lane) : 0x7fffffff;
+        const int o = lane < S ? __ldg(c.off + lane) : 0x7fffffff, cx = lane < S ? __ldg(c.ctx + lane) : 0;
+        const int next = __shfl_down_sync(0xffffffffu, o, 1);
+        good = __all_sync(0xffffffffu, lane >= S || good_stream(c, lane, o, lane + 1 < S ? next : last, cx));
 #pragma unroll
         for (int k = 16; k; k >>= 1) {
             const int v = __shfl_sync(0xffffffffu, o, s + k);
@@ -39,6 +47,7 @@ __device__ RowAt row_at(const ChunkP &c, const KvP &kv, Ctrl *ctrl, long long r)
         o0 = __shfl_sync(0xffffffffu, o, s);
         o1 = __shfl_sync(0xffffffffu, o, (s + 1) & 31);
         if (s + 1 >= S) o1 = last;
+        ctx = __shfl_sync(0xffffffffu, cx, s);
     } else {
         int hi = S;
         while (hi - s > 1) {
@@ -47,18 +56,15 @@ __device__ RowAt row_at(const ChunkP &c, const KvP &kv, Ctrl *ctrl, long long r)
         }
         o0 = __ldg(c.off + s);
         o1 = __ldg(c.off + s + 1);
+        ctx = __ldg(c.ctx + s);
     }
     RowAt a{-1, -1};
-    if (r >= c.n_rows || (desc && r >= last)) return a;  // none, or behind the last sequence
-    bool bad = !desc || o0 < 0 || o0 > r || o1 <= r || o1 > last;
+    if (r >= c.n_rows || (good && r >= last)) return a;  // none, or behind the last sequence
+    bool bad = !good || !good_stream(c, s, o0, o1, ctx) || o0 > r || o1 <= r;
     if (!bad) {
-        const int ctx = __ldg(c.ctx + s);
-        bad = ctx < 0 || (long long)ctx + (o1 - o0) > c.max_pos;
-        if (!bad) {
-            const int pos = ctx + (int)(r - o0), ph = __ldg(kv.table + (long long)s * c.max_pages + pos / 64);
-            bad = ph < 0 || ph >= kv.n_pages;
-            if (!bad) a = RowAt{pos, ph};
-        }
+        const int pos = ctx + (int)(r - o0), ph = __ldg(kv.table + (long long)s * c.max_pages + pos / 64);
+        bad = ph < 0 || ph >= kv.n_pages;
+        if (!bad) a = RowAt{pos, ph};
     }
     if (bad) raise(ctrl, MK_ERR_BAD_INPUT, 401);
     return a;
@@ -98,14 +104,21 @@ __device__ __forceinline__ Share share_of(int rb) {
 // looked up by every warp for itself: no barrier in the shortest calls.
 __device__ __forceinline__ bool rows_of(const ChunkP &c, const KvP &kv, Ctrl *ctrl, long long r0, int rb, RowAt (*at)[32]) {
     const int lane = threadIdx.x % 32, wid = threadIdx.x / 32;
+    bool good = true;
+    if (c.S > 32) {
+        bool bad = false;
+        for (int i = threadIdx.x; i < c.S; i += 256)
+            bad |= !good_stream(c, i, __ldg(c.off + i), __ldg(c.off + i + 1), __ldg(c.ctx + i));
+        good = !__syncthreads_or(bad);
+    }
     if (rb == 1) {
-        const RowAt a = row_at(c, kv, ctrl, lane < 1 ? r0 : c.n_rows);
+        const RowAt a = row_at(c, kv, ctrl, lane < 1 ? r0 : c.n_rows, good);
         at[wid][lane] = a;
         __syncwarp();
         return !__any_sync(0xffffffffu, aborted(ctrl));
     }
     if (wid == 0) {
-        const RowAt a = row_at(c, kv, ctrl, lane < rb ? r0 + lane : c.n_rows);
+        const RowAt a = row_at(c, kv, ctrl, lane < rb ? r0 + lane : c.n_rows, good);
         at[0][lane] = a;
     }
     return !__syncthreads_or(threadIdx.x == 0 && aborted(ctrl));
