@@ -492,6 +492,7 @@ attn_mma_kernel(const __grid_constant__ MmaP p, const __grid_constant__ CUtensor
                     }
                     stat[r] = m;
                     stat[128 + r] = l;
+                    fence_async();                              // the next unit's Q comes by TMA to the same bytes
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive(bdone);
@@ -548,6 +549,7 @@ attn_mma_kernel(const __grid_constant__ MmaP p, const __grid_constant__ CUtensor
             }
             if (chk != 0.f) p.ws.odd[blockIdx.x] = 1;
             if (dual) {
+                fence_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive(adone);               // the Q tiles are free again
             }
