@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(JT, 3) attn_join_kernel(AttnWs ws, Ctrl *ctrl,
             }
             __syncthreads();
         }
-    }    const bool own = __any_sync(0xffffffffu, chk != 0.f);
+    }
+    const bool own = __any_sync(0xffffffffu, chk != 0.f);
     if (own || odd) rows_again<D, Act, KV>(g, out, cut, upto, base, n_cta, own, odd);
 }
 

@@ -31,11 +31,13 @@
 // at the box's end and the rest is TMA's zero fill, for K and V alike.
 //
 // Measured (32/4 heads, one GB300; of the copy bandwidth and the cuBLAS bf16 rate):
-//   one prompt of 8192 tokens, bf16      382 us   1.44 PFLOP/s, 73 %: the chain S -> softmax
+//   one prompt of 8192 tokens, bf16      384 us   1.43 PFLOP/s, 73 %: the chain S -> softmax
 //                                                 -> P -> O of two tiles, whose waits leave the
 //                                                 tensor cores idle for 30 % of the kernel
-//   chunks up to 2048, FP8 cache         192 us   1.07 PFLOP/s, 55 %: shared memory, which the
-//                                                 widening of the codes loads once more
+//   chunks up to 2048, FP8 cache         191 us   1.08 PFLOP/s, 55 %: 3950 cycles per 128 keys of
+//                                                 two tiles, against 2048 of MMAs and some 2500
+//                                                 of shared memory; the widening of the codes
+//                                                 lies between their arrival and the MMAs
 //   16 single tokens, bf16 cache          39 us   4.0 TB/s, 59 %: this kernel 32 us (4.9 TB/s)
 //   6 tokens over 65536, FP8 cache        33 us   2.0 TB/s, 30 %: this kernel 27 us; the
 //                                                 widening is 1500 of 2900 cycles per 128 keys
@@ -60,8 +62,9 @@ struct Cfg {
     // as OV iterations (an FP8 cache's include the conversion of Q).  Measured with 2,
     // 3, 4, 5: a prompt of 8192 tokens, bf16, 391, 387, 388, 391 us; chunks up to 2048
     // over FP8 216, 200, 196, 192.  A CTA takes MIN_COST at least, so that small calls
-    // are not cut to pieces: their mean over 44 drawn calls is 29.3 us with OV + 1,
-    // 29.0 with OV, 29.3 with OV - 1; 137 tokens alone 20.5 with OV + 2, 14.4 with OV.
+    // are not cut to pieces: the mean of 44 calls of 1 to 16 streams of random lengths and
+    // contexts is 29.3 us with OV + 1, 29.0 with OV, 29.3 with OV - 1; 137 tokens alone
+    // take 20.5 with OV + 2, 14.4 with OV.
     static constexpr int OV = FP8 ? 5 : 3, MIN_COST = OV;
     // A row's reference maximum moves when its maximum has grown by more than GROW powers
     // of two, and its probabilities, their sum and its output are held times 2^BIAS, which
